@@ -18,6 +18,7 @@
 #include "cstore.cuh"
 #include "head.h"
 #include "ptx.cuh"
+#include "row_blocks.h"
 
 namespace gb300 {
 
@@ -60,7 +61,7 @@ __device__ __forceinline__ uint4 load8(const uint16_t* p, int64_t valid, uintptr
     const uint32_t shift = static_cast<uint32_t>(at & 15);
     const uintptr_t block = at - shift;
     if (valid >= 8 && shift == 0) return __ldg(reinterpret_cast<const uint4*>(p));
-    if (block >= lo && block + 32 <= hi)
+    if (pair_inside(at, lo, hi))
         return cut8(__ldg(reinterpret_cast<const uint4*>(block)), __ldg(reinterpret_cast<const uint4*>(block + 16)),
                     shift, valid);
     uint32_t o[4];
@@ -213,7 +214,7 @@ __global__ void __launch_bounds__(256) pack_rows_kernel(const uint16_t* in, int6
     for (int64_t i = blockIdx.x * 8ll + (threadIdx.x >> 5); i < rows; i += gridDim.x * 8ll) {
         const uint16_t* from = in + i * ld;
         uint16_t* to = out + i * ldc;
-        if (i == 0 || i == rows - 1) {   // blocks partly outside the matrix
+        if (!row_inside(reinterpret_cast<uintptr_t>(from), cols, lo, hi)) {   // near the matrix's ends
             for (int64_t c = lane * 8; c < ldc; c += 256)
                 *reinterpret_cast<uint4*>(to + c) =
                     c < cols ? load8(from + c, cols - c, lo, hi) : make_uint4(0, 0, 0, 0);
