@@ -100,7 +100,10 @@ __global__ void __launch_bounds__(kGatherThreads) gather_kernel(const GatherArgs
         if (!has_target(r, i)) continue;
         ++total;
         before += i < first;
-        if (a.lse) top = fmaxf(top, fabsf(a.grad_loss[static_cast<int64_t>(i) * a.grad_stride]));
+        if (a.lse) {
+            const float size = fabsf(a.grad_loss[static_cast<int64_t>(i) * a.grad_stride]);
+            if (isfinite(size)) top = fmaxf(top, size);
+        }
     }
 #pragma unroll
     for (int o = 16; o; o >>= 1) {
@@ -124,7 +127,7 @@ __global__ void __launch_bounds__(kGatherThreads) gather_kernel(const GatherArgs
     }
     if (blockIdx.x == 0 && tid == 0) {
         *r.count = total;
-        if (a.lse) *a.factor = top * a.undo;
+        if (a.lse) *a.factor = top > 0.0f ? top * a.undo : a.undo;
     }
     const int zero_end = (total + a.pad_rows - 1) / a.pad_rows * a.pad_rows;
     const uintptr_t lo = reinterpret_cast<uintptr_t>(a.hidden);
@@ -158,7 +161,8 @@ __global__ void __launch_bounds__(kGatherThreads) gather_kernel(const GatherArgs
                 const float l = a.lse[i];
                 a.lse2[place] = l * kLog2e;
                 // divided first: the largest may be close to the smallest
-                // numbers there are; without a largest, zeros and NaN stay
+                // numbers there are; infinities and NaN stay, and so do
+                // zeros where there is no largest
                 const float own = a.grad_loss[static_cast<int64_t>(i) * a.grad_stride];
                 a.gain[place] = top > 0.0f ? own / top * a.unit : own;
                 a.boost[place] = 1.0f + 2.0f * a.z_loss * l;
