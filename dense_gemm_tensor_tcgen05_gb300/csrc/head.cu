@@ -74,6 +74,12 @@ __device__ __forceinline__ uint4 load8(const uint16_t* p, int64_t valid, uintptr
     return make_uint4(o[0], o[1], o[2], o[3]);
 }
 
+// d loss / d z = p (1 + t) - y with t = 2 z_loss lse: p and y are in [0, 1], so
+// it is at most 1 + |t| in size.
+__device__ __forceinline__ float z_term(const GatherArgs& a, int i) {
+    return a.z_loss > 0.0f ? 2.0f * a.z_loss * a.lse[i] : 0.0f;
+}
+
 // ---- the compact order --------------------------------------------------------
 //
 // Every block counts all targets (they sit in L2 after the first block's
@@ -101,7 +107,8 @@ __global__ void __launch_bounds__(kGatherThreads) gather_kernel(const GatherArgs
         ++total;
         before += i < first;
         if (a.lse) {
-            const float size = fabsf(a.grad_loss[static_cast<int64_t>(i) * a.grad_stride]);
+            const float size =
+                fabsf(a.grad_loss[static_cast<int64_t>(i) * a.grad_stride]) * (1.0f + fabsf(z_term(a, i)));
             if (isfinite(size)) top = fmaxf(top, size);
         }
     }
@@ -158,14 +165,13 @@ __global__ void __launch_bounds__(kGatherThreads) gather_kernel(const GatherArgs
             if (act && !r.distill)
                 r.target_c[place] = static_cast<int32_t>(r.target[static_cast<int64_t>(i) * r.target_stride]);
             if (act && a.lse) {
-                const float l = a.lse[i];
-                a.lse2[place] = l * kLog2e;
+                a.lse2[place] = a.lse[i] * kLog2e;
                 // divided first: the largest may be close to the smallest
                 // numbers there are; infinities and NaN stay, and so do
                 // zeros where there is no largest
                 const float own = a.grad_loss[static_cast<int64_t>(i) * a.grad_stride];
                 a.gain[place] = top > 0.0f ? own / top * a.unit : own;
-                a.boost[place] = 1.0f + 2.0f * a.z_loss * l;
+                a.boost[place] = 1.0f + z_term(a, i);
             }
         }
         __syncthreads();

@@ -48,12 +48,13 @@ __device__ __forceinline__ int32_t head_target(const int64_t* target, int64_t st
 // 8; the columns from dim to ldc are zeros) and fills HeadRows' order.  The
 // rows from *count up to the next multiple of pad_rows are zeros.  With lse
 // (backward), it also lays out by place what the logits' gradient takes:
-// lse2 = lse log2 e, gain = grad_loss / max |grad_loss| * unit and
-// boost = 1 + 2 z_loss lse, and writes the factor that undoes the gain's
-// scaling, factor = max |grad_loss| * undo.  The largest is that of the
-// finite ones: an infinite or NaN grad_loss stays with its token's row, and
-// with the sums that the row goes into.  With zero_rows, the rows there of
-// tokens without a target are zeroed (element type zero_ct).
+// lse2 = lse log2 e, gain = grad_loss / top * unit and boost = 1 + 2 z_loss
+// lse, and writes the factor that undoes the gain's scaling, factor = top *
+// undo.  top is the largest |grad_loss| (1 + |2 z_loss lse|), which bounds a
+// token's gradient of the logits, so that none passes unit in size.  It is
+// the largest of the finite ones: an infinite or NaN grad_loss stays with its
+// token's row, and with the sums that the row goes into.  With zero_rows, the
+// rows there of tokens without a target are zeroed (element type zero_ct).
 struct GatherArgs {
     HeadRows rows;
     const uint16_t* hidden;

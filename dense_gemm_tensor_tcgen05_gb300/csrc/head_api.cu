@@ -445,11 +445,10 @@ gemm_status_t backward(const gemm_head_t* head, int distill, const float* lse, c
     GB_TRY(check_overlap(h, distill, more, 2, outs, 3));
     GB_TRY(lib_device(&dev, &sms));
 
-    // d loss / d logits is at most 1 in size (with a z term, 1 + 2 z_loss
-    // lse); FP16 holds it times 2^14 (2^10 with a z term), so that the
-    // probabilities down to 2^-28 (2^-24) stay normal numbers and the largest
-    // stays in range.  BF16 has FP32's range and needs no unit.
-    const float unit = h.dtype == 1 ? 1.0f : (!distill && h.z_loss > 0.0f) ? 1024.0f : 16384.0f;
+    // The gather scales the logits' gradient to at most 1 in size; FP16 holds
+    // it times 2^14, so that probabilities down to 2^-28 of the largest stay
+    // normal numbers.  BF16 has FP32's range and needs no unit.
+    const float unit = h.dtype == 1 ? 1.0f : 16384.0f;
     GatherArgs g;
     memset(&g, 0, sizeof(g));
     g.pad_rows = kHeadStepK;

@@ -70,3 +70,67 @@ def test_all_weights_infinite(g):
     dh, dw = g.linear_cross_entropy_backward(torch.full((1,), math.inf, device="cuda"), H, W, t, lse)
     done(g)
     assert not torch.isfinite(dh).any() and not torch.isfinite(dw).any()
+
+
+class Gradients:
+    """dhidden and dweight of the cross entropy in 64 bits (CPU) for any z
+    term, with bounds.
+
+    z and lse are off by dz and dlse as in head_ref.py.  The logits' gradient
+    of token n is G = k (p (1 + t) - y), k = grad_loss scale, t = 2 z_loss lse,
+    at most S_n = |k| (1 + |t|) in size; the errors of p and t move it by
+
+        |k| (p |1 + t| (dz + dlse + 2^-20) + 2 z_loss p dlse)
+
+    and FP32 by 2^-22 of its terms.  It is rounded to 16 bits: u of itself,
+    and in FP16 at least half a step of 2^-24 in the unit 2^-14 max S."""
+
+    def __init__(self, H, W, t, gl, z_loss, grad_dtype, scale=1.0):
+        ty = H.dtype
+        H, W, t = H.cpu().double(), W.cpu().double(), t.cpu()
+        N, D = H.shape
+        V = W.shape[0]
+        k = gl.cpu().double().expand(N) * scale
+        z = (H @ W.T) * scale
+        lse = torch.logsumexp(z, 1)
+        y = torch.zeros(N, V, dtype=torch.float64).scatter_(1, t[:, None], 1.0)
+        p = torch.exp(z - lse[:, None])
+        term = 2.0 * z_loss * lse
+        G = (p * (1.0 + term)[:, None] - y) * k[:, None]
+        self.dhidden, self.dweight = G @ W, G.T @ H
+        dz = ref.acc(D) * (H.abs() @ W.abs().T) * scale + 2.0 ** -22 * z.abs()
+        dlse = (dz.amax(1) + 2.0 ** -15 + 2.0 ** -21 * z.abs().amax(1))[:, None]
+        size, K = (1.0 + term).abs()[:, None], k.abs()[:, None]
+        S = K * (1.0 + term.abs())[:, None]
+        u, go = ref.U[ty], ref.U[grad_dtype]
+        step = 0.0 if ty == BF16 else 2.0 ** -39 * S.max()
+        dG = K * p * (size * (dz + dlse + 2.0 ** -20) + 2.0 * z_loss * dlse) + 2.0 ** -22 * K * (p * size + y) \
+            + u * G.abs() + step + 2.0 ** -125 * (S + 1)
+        tiny = 2.0 ** -25 if grad_dtype == F16 else 2.0 ** -125
+        self.tol = {
+            "dhidden": (dG + ref.acc(V) * G.abs()) @ W.abs() * (1 + go) + (go + 2.0 ** -22) * self.dhidden.abs() + tiny,
+            "dweight": (dG + ref.acc(N) * G.abs()).T @ H.abs() * (1 + go) + (go + 2.0 ** -22) * self.dweight.abs() + tiny,
+        }
+
+    check = ref.Reference.check
+
+
+@pytest.mark.parametrize("dtype", [BF16, F16], ids=["bf16", "f16"])
+@pytest.mark.parametrize("N", [70, 300])
+@pytest.mark.parametrize("z_loss,spread,shift", [(1.0, 20.0, 0.0), (0.1, 120.0, 0.0), (1.0, 1.5, -256.0),
+                                                 (10.0, 1.5, 256.0), (1e-4, 1.5, 0.0)],
+                         ids=["1", "0.1-wide", "negative", "10-large", "usual"])
+def test_z_terms_of_any_size(g, z_loss, spread, shift, N, dtype):
+    # 1 + 2 z_loss lse from -500 to 5000: the logits' gradient passes FP16's
+    # range many times, the gradients themselves are ordinary numbers
+    H, W, t, gl = ref.inputs(N, 700, 64, dtype, 73, spread=spread)
+    if shift:                              # a channel that moves all logits
+        H[:, 0] = 8.0
+        W[:, 0] = shift / 8.0
+    gl *= 1e-3
+    loss, lse = g.linear_cross_entropy(H, W, t, z_loss=z_loss)
+    dh, dw = g.linear_cross_entropy_backward(gl, H, W, t, lse, z_loss=z_loss, grad_dtype=F32)
+    done(g)
+    r = Gradients(H, W, t, gl, z_loss, F32)
+    r.check("dhidden", dh)
+    r.check("dweight", dw)
