@@ -92,7 +92,7 @@ __global__ void __launch_bounds__(kGatherThreads) gather_kernel(const GatherArgs
     grid_dep_launch_dependents();
     grid_dep_wait();
     __shared__ int s_before[8], s_total[8], s_warp[8];
-    __shared__ float s_top[8];
+    __shared__ float s_top[8], s_low[8];
     __shared__ int s_rank[kGatherThreads];
     const HeadRows& r = a.rows;
     const int n = static_cast<int>(r.tokens);
@@ -101,7 +101,7 @@ __global__ void __launch_bounds__(kGatherThreads) gather_kernel(const GatherArgs
     const int last = min(n, first + rows_per_block);
 
     int before = 0, total = 0;
-    float top = 0.0f;
+    float top = 0.0f, low = INFINITY;   // of the sizes that are finite and not 0
     for (int i = tid; i < n; i += kGatherThreads) {
         if (!has_target(r, i)) continue;
         ++total;
@@ -110,6 +110,7 @@ __global__ void __launch_bounds__(kGatherThreads) gather_kernel(const GatherArgs
             const float size =
                 fabsf(a.grad_loss[static_cast<int64_t>(i) * a.grad_stride]) * (1.0f + fabsf(z_term(a, i)));
             if (isfinite(size)) top = fmaxf(top, size);
+            if (size > 0.0f) low = fminf(low, size);
         }
     }
 #pragma unroll
@@ -117,8 +118,10 @@ __global__ void __launch_bounds__(kGatherThreads) gather_kernel(const GatherArgs
         before += __shfl_xor_sync(~0u, before, o);
         total += __shfl_xor_sync(~0u, total, o);
         top = fmaxf(top, __shfl_xor_sync(~0u, top, o));
+        low = fminf(low, __shfl_xor_sync(~0u, low, o));
     }
     if (lane == 0) {
+        s_low[warp] = low;
         s_before[warp] = before;
         s_total[warp] = total;
         s_top[warp] = top;
@@ -126,15 +129,22 @@ __global__ void __launch_bounds__(kGatherThreads) gather_kernel(const GatherArgs
     __syncthreads();
     before = total = 0;
     top = 0.0f;
+    low = INFINITY;
 #pragma unroll
     for (int w = 0; w < 8; ++w) {
+        low = fminf(low, s_low[w]);
         before += s_before[w];
         total += s_total[w];
         top = fmaxf(top, s_top[w]);
     }
+    const bool spread = a.by_row && low < top / kHeadSpread;
+    const float factor = top > 0.0f ? top * a.undo : a.undo;
     if (blockIdx.x == 0 && tid == 0) {
         *r.count = total;
-        if (a.lse) *a.factor = top > 0.0f ? top * a.undo : a.undo;
+        if (a.lse) {
+            *a.factor = factor;
+            *a.spread = spread;
+        }
     }
     const int zero_end = (total + a.pad_rows - 1) / a.pad_rows * a.pad_rows;
     const uintptr_t lo = reinterpret_cast<uintptr_t>(a.hidden);
@@ -170,8 +180,16 @@ __global__ void __launch_bounds__(kGatherThreads) gather_kernel(const GatherArgs
                 // numbers there are; infinities and NaN stay, and so do
                 // zeros where there is no largest
                 const float own = a.grad_loss[static_cast<int64_t>(i) * a.grad_stride];
-                a.gain[place] = top > 0.0f ? own / top * a.unit : own;
-                a.boost[place] = 1.0f + z_term(a, i);
+                const float term = z_term(a, i), most = 1.0f + fabsf(term);
+                if (spread) {
+                    a.gain[place] = a.unit / most;
+                    a.undo_row[place] = own * most * a.undo;
+                    a.ratio[place] = own * most / top;
+                } else {
+                    a.gain[place] = top > 0.0f ? own / top * a.unit : own;
+                    a.undo_row[place] = factor;
+                }
+                a.boost[place] = 1.0f + term;
             }
         }
         __syncthreads();
@@ -430,7 +448,7 @@ __global__ void __launch_bounds__(256) sum_rows_kernel(const SumRowsArgs a, bool
     grid_dep_wait();
     const int64_t quads = (a.cols + 3) >> 2;
     const int64_t all = a.rows * quads;
-    const float factor = *a.factor;
+    const float all_rows = a.row_factor ? 0.0f : *a.factor;
     const int count = a.rank ? *a.count : 0;
     for (int64_t x = blockIdx.x * 256ll + threadIdx.x; x < all; x += gridDim.x * 256ll) {
         const int64_t i = x / quads, c = (x - i * quads) * 4;
@@ -450,6 +468,7 @@ __global__ void __launch_bounds__(256) sum_rows_kernel(const SumRowsArgs a, bool
                 v.z += t.z;
                 v.w += t.w;
             }
+            const float factor = a.row_factor ? a.row_factor[from] : all_rows;
             v.x *= factor;
             v.y *= factor;
             v.z *= factor;

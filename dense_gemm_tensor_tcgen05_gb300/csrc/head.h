@@ -50,11 +50,19 @@ __device__ __forceinline__ int32_t head_target(const int64_t* target, int64_t st
 // (backward), it also lays out by place what the logits' gradient takes:
 // lse2 = lse log2 e, gain = grad_loss / top * unit and boost = 1 + 2 z_loss
 // lse, and writes the factor that undoes the gain's scaling, factor = top *
-// undo.  top is the largest |grad_loss| (1 + |2 z_loss lse|), which bounds a
-// token's gradient of the logits, so that none passes unit in size.  It is
-// the largest of the finite ones: an infinite or NaN grad_loss stays with its
-// token's row, and with the sums that the row goes into.  With zero_rows, the
-// rows there of tokens without a target are zeroed (element type zero_ct).
+// undo, also for each row (undo_row).  top is the largest of size = |grad_loss|
+// (1 + |2 z_loss lse|), which bounds a token's gradient of the logits, so that
+// none passes unit in size.  It is the largest of the finite ones: an infinite
+// or NaN grad_loss stays with its token's row, and with the sums that the row
+// goes into.
+// by_row (a type with few exponents, and dhidden is wanted): where sizes
+// differ by more than kHeadSpread, a row of dhidden would be summed from
+// numbers that fall below the type's normal ones.  *spread is then 1, every
+// row has a gain of its own, unit / (1 + |2 z_loss lse|), undone by
+// undo_row, and ratio turns it into the gain relative to top, which dweight
+// needs, as its sums run over rows.
+// With zero_rows, the rows there of tokens without a target are zeroed
+// (element type zero_ct).
 struct GatherArgs {
     HeadRows rows;
     const uint16_t* hidden;
@@ -66,11 +74,14 @@ struct GatherArgs {
     const float* grad_loss;
     int64_t grad_stride;
     float z_loss, unit, undo;
-    float *lse2, *gain, *boost, *factor;
+    float *lse2, *gain, *boost, *factor, *undo_row, *ratio;
+    int by_row;
+    int32_t* spread;
     void* zero_rows;
     int64_t ld_zero;
     int zero_ct;
 };
+constexpr float kHeadSpread = 16.0f;
 cudaError_t gather_launch(const GatherArgs& a, int sms, cudaStream_t stream);
 
 struct TeacherArgs {
@@ -111,8 +122,9 @@ struct JoinArgs {
 };
 cudaError_t join_launch(const JoinArgs& a, cudaStream_t stream);
 
-// out[i][j] = factor * sum_s parts[s][row(i)][j], row(i) = rank[i] if rank
-// (and zeros where that is not below *count), else i.
+// out[i][j] = f * sum_s parts[s][row(i)][j], row(i) = rank[i] if rank (and
+// zeros where that is not below *count), else i; f = row_factor[row(i)] if
+// row_factor, else *factor.
 struct SumRowsArgs {
     void* out;
     int ct;   // 0 FP32, 1 FP16, 2 BF16
@@ -123,6 +135,7 @@ struct SumRowsArgs {
     const int32_t* rank;
     const int32_t* count;
     const float* factor;
+    const float* row_factor;
 };
 cudaError_t sum_rows_launch(const SumRowsArgs& a, int sms, cudaStream_t stream);
 

@@ -142,7 +142,8 @@ struct Layout {
     int64_t bytes = 0;
     int64_t dp, piece, np, tiles;   // padded dim, words of a piece, padded tokens
     int64_t count, factor, perm, rank, target_c, words, logq, active, lse2, gain, boost, z_at, stats, zsum;
-    int64_t hidden = 0, weight, grad, dh, dw;
+    int64_t undo_row, ratio, spread;
+    int64_t hidden = 0, weight, grad, by_row, dh, dw;
     int h_slices, w_slices;
     bool h_direct;      // dhidden needs no sum of parts: one piece, one slice
     bool pack_weight;
@@ -171,7 +172,8 @@ Layout layout_of(const gemm_head_t& h, int distill, int backward) {
     l.perm = take(4 * n);
     l.rank = take(4 * n);
     l.target_c = l.words = l.logq = l.active = 0;
-    l.lse2 = l.gain = l.boost = l.z_at = l.stats = l.zsum = l.grad = l.dh = l.dw = l.weight = 0;
+    l.lse2 = l.gain = l.boost = l.z_at = l.stats = l.zsum = l.grad = l.by_row = l.dh = l.dw = l.weight = 0;
+    l.undo_row = l.ratio = l.spread = 0;
     l.h_slices = l.w_slices = 1;
     l.h_direct = false;
     // A forward call of up to one tile of tokens saves no product by leaving
@@ -196,7 +198,12 @@ Layout layout_of(const gemm_head_t& h, int distill, int backward) {
         l.lse2 = take(4 * n);
         l.gain = take(4 * n);
         l.boost = take(4 * n);
+        l.undo_row = take(4 * n);
+        l.ratio = take(4 * n);
+        l.spread = take(4);
         l.grad = take(2 * n * l.piece);
+        // FP16: the copy with a scale for each row, written where weights differ much
+        if (h.dtype == 0) l.by_row = take(2 * n * l.piece);
         const int64_t dim_tiles = ceil_div(h.dim, kHeadTileN);
         const Slices both = slices(products_together(h), ceil_div(n, kHeadTileM) * dim_tiles,
                                    l.piece / kHeadStepK, l.piece < h.vocab, l.piece / kHeadTileM * dim_tiles,
@@ -463,6 +470,10 @@ gemm_status_t backward(const gemm_head_t* head, int distill, const float* lse, c
     g.gain = at<float>(ws, l.gain);
     g.boost = at<float>(ws, l.boost);
     g.factor = at<float>(ws, l.factor);
+    g.undo_row = at<float>(ws, l.undo_row);
+    g.ratio = at<float>(ws, l.ratio);
+    g.spread = at<int32_t>(ws, l.spread);
+    g.by_row = h.dtype == 0 && want_h;
     if (want_h && l.h_direct) {
         g.zero_rows = dhidden;
         g.ld_zero = lddh;
@@ -487,6 +498,12 @@ gemm_status_t backward(const gemm_head_t* head, int distill, const float* lse, c
     d.ct = h.dtype == 1 ? kCBF16 : kCF16;
     d.out_inner = d.ldo = l.piece;
     d.out_outer = h.tokens;
+    // without dweight the only copy is the one by rows
+    if (g.by_row && want_w) {
+        d.spread = g.spread;
+        d.by_row = at<uint16_t>(ws, l.by_row);
+        d.ratio = g.ratio;
+    }
 
     HeadGemm ph;   // dhidden = gradient weight, summed over the pieces
     memset(&ph, 0, sizeof(ph));
@@ -499,6 +516,8 @@ gemm_status_t backward(const gemm_head_t* head, int distill, const float* lse, c
     ph.splits = l.h_slices;
     ph.chunk = kChunk;
     ph.p.kmajor = 1;
+    ph.spread = d.spread;
+    ph.by_row = d.by_row;
     if (l.h_direct) {   // straight to the tokens' rows
         ph.out = dhidden;
         ph.ct = ct;
@@ -506,7 +525,7 @@ gemm_status_t backward(const gemm_head_t* head, int distill, const float* lse, c
         ph.ldo = lddh;
         ph.out_outer = h.tokens;
         ph.out_perm = g.rows.perm;
-        ph.factor = g.factor;
+        ph.row_factor = g.undo_row;
     } else {
         ph.out = at<float>(ws, l.dh);
         ph.ct = kCF32;
@@ -592,6 +611,7 @@ gemm_status_t backward(const gemm_head_t* head, int distill, const float* lse, c
         s.part_stride = l.np * l.dp;
         s.rank = g.rows.rank;
         s.count = g.rows.count;
+        s.row_factor = g.undo_row;
         GB_TRY(lib_launch_status(sum_rows_launch(s, sms, stream), "sum_rows"));
     }
     return GEMM_OK;

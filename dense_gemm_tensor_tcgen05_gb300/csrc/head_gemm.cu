@@ -97,7 +97,9 @@ struct Args {
     int64_t ldo;
     int32_t ct, tensor_store, add, out_rows, out_cols, split_rows;
     const int32_t* out_perm;   // row r goes to out_perm[r], or NULL
-    const float* factor;
+    const float *factor, *row_factor;
+    const int32_t* spread;
+    const float* ratio;
     // loss
     const int32_t* target_c;
     const int64_t* target;   // read where there is no order (perm NULL)
@@ -114,9 +116,10 @@ struct Args {
     const float *lse2, *gain, *boost;
 };
 
-// One product: its operands' and output's tensor maps and its arguments.
+// One product: its operands' and output's tensor maps (by_row: of the copy of
+// the logits' gradient that has a scale for each row) and its arguments.
 struct Params {
-    CUtensorMap p, q, o;
+    CUtensorMap p, q, o, by_row;
     Args a;
 };
 
@@ -602,6 +605,8 @@ head_gemm_kernel(const __grid_constant__ Params first, const __grid_constant__ P
             if (lane == 0) {
                 const Work w1(first.a), w2 = kTwo ? Work(second.a) : Work();
                 Turns turns(w1, w1.steps / first.a.splits, w2, kTwo && second.a.splits ? w2.steps / second.a.splits : 0);
+                const bool alt1 = MODE == kHeadProduct && first.a.spread && *first.a.spread;
+                const bool alt2 = kTwo && second.a.spread && *second.a.spread;
                 bool two;
                 int u;
                 int stage = 0;
@@ -616,7 +621,8 @@ head_gemm_kernel(const __grid_constant__ Params first, const __grid_constant__ P
                     // every other unit walks K backwards: it starts on the operand
                     // slices that the wave before it read last (still in L2)
                     const bool down = (items++ & 1) != 0;
-                    const CUtensorMap* map = p_side ? &x.p : &x.q;
+                    const bool alt = kTwo && two ? alt2 : alt1;
+                    const CUtensorMap* map = !p_side ? &x.q : alt ? &x.by_row : &x.p;
                     const bool kmajor = p_side ? a.p_kmajor : a.q_kmajor;
                     for (int s = it.k0; s < it.k1; ++s) {
                         const int ks = down ? it.k1 - 1 - (s - it.k0) : s;
@@ -732,6 +738,7 @@ head_gemm_kernel(const __grid_constant__ Params first, const __grid_constant__ P
         const uint32_t lanes = (static_cast<uint32_t>(quarter * 32) << 16) + static_cast<uint32_t>(half * kCols);
         const float factor1 = MODE == kHeadProduct && first.a.factor ? *first.a.factor : 1.0f;
         const float factor2 = kTwo && second.a.factor ? *second.a.factor : 1.0f;
+        const bool spread = kGrad && first.a.spread && *first.a.spread;
         int acc = 0;
         uint32_t acc_phase = 0;
         bool ok = true;
@@ -746,12 +753,15 @@ head_gemm_kernel(const __grid_constant__ Params first, const __grid_constant__ P
             const bool some = row0 < w.m && col0 < a.n;   // of this warp's results are wanted
             const int32_t word0 = a.w0 + col0;
             Hits hits;
-            float lse2 = 0.0f, gain = 0.0f, boost = 0.0f;
+            float lse2 = 0.0f, gain = 0.0f, boost = 0.0f, ratio = 0.0f;
+            float factor = kTwo && two ? factor2 : factor1;
+            if (MODE == kHeadProduct && a.row_factor && row < w.m) factor = a.row_factor[row];
             if (!kKd && (kStats || kGrad) && row < w.m) hits.start<kKd>(a, row, word0);
             if (kGrad && row < w.m) {
                 lse2 = a.lse2[row];
                 gain = a.gain[row];
                 boost = a.boost[row];
+                if (spread) ratio = a.ratio[row];
             }
             float v[kCols];
             if (it.k0 == it.k1) {   // the empty sum
@@ -895,10 +905,14 @@ head_gemm_kernel(const __grid_constant__ Params first, const __grid_constant__ P
                     for (int i = 0; i < kCols; ++i) v[i] = i < wide ? v[i] : 0.0f;
                 }
                 __syncwarp();
-                store_boxes(Out(a), &x.o, box, box, v, lane, row0, row0, col0);
+                const Out to(a);
+                if (spread) {   // the copy with a scale for each row, then the common one
+                    store_boxes(to, &x.by_row, box, box, v, lane, row0, row0, col0);
+                    scale_all(v, ratio);
+                }
+                store_boxes(to, &x.o, box, box, v, lane, row0, row0, col0);
             } else {
                 if (!some) continue;
-                const float factor = kTwo && two ? factor2 : factor1;
                 const Out to(a);
                 const bool tensor_store = a.tensor_store;
                 const int split_rows = a.split_rows;
@@ -1008,7 +1022,15 @@ static bool params_of(const HeadGemm& g, int p_rows, int stages, EncodeTiledFn f
                     CU_TENSOR_MAP_L2_PROMOTION_NONE))
             return false;
         a.tensor_store = 1;
+        if (g.by_row && g.mode != kHeadProduct &&
+            !encode(fn, &x->by_row, t, es, g.by_row, g.out_inner, g.out_outer, g.ldo, static_cast<uint32_t>(128 / es),
+                    32, CU_TENSOR_MAP_L2_PROMOTION_NONE))
+            return false;
     }
+    if (g.by_row && g.mode == kHeadProduct &&
+        !encode(fn, &x->by_row, t16, 2, g.by_row, g.p.inner, g.p.outer, g.p.ld, 64, box_p,
+                CU_TENSOR_MAP_L2_PROMOTION_L2_256B))
+        return false;
     // slices, sums onto the output and the logits' gradient leave through tensor stores only
     if (!a.tensor_store && (g.splits > 1 || g.add || g.mode == kHeadGradCe || g.mode == kHeadGradKd)) return false;
     a.m = static_cast<int32_t>(g.m);
@@ -1036,6 +1058,9 @@ static bool params_of(const HeadGemm& g, int p_rows, int stages, EncodeTiledFn f
     a.split_rows = static_cast<int32_t>(g.split_rows);
     a.out_perm = g.out_perm;
     a.factor = g.factor;
+    a.row_factor = g.row_factor;
+    a.spread = g.by_row ? g.spread : nullptr;
+    a.ratio = g.ratio;
     a.target_c = g.rows.target_c;
     a.target = g.rows.target;
     a.target_stride = g.rows.target_stride;

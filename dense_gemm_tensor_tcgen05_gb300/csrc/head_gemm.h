@@ -45,6 +45,13 @@ struct HeadGemm {
     int add;                 // add to the output (FP32, tensor stores only)
     const int32_t* out_perm; // products: row r goes to row out_perm[r], or NULL
     const float* factor;     // products: multiply by *factor, or NULL
+    const float* row_factor; // products: multiply row r by row_factor[r], or NULL
+    // Where *spread is not 0 (NULL: never), the logits' gradient goes to
+    // by_row as it is and to out times ratio[r] in row r; a product takes P
+    // from by_row, which is laid out as p.
+    const int32_t* spread;
+    void* by_row;
+    const float* ratio;
     // the loss
     HeadRows rows;
     int64_t w0;              // first word

@@ -242,7 +242,7 @@ def linear_cross_entropy_backward(grad_loss, hidden, weight, target, lse, *, ign
     the forward call.  Gradients have hidden's dtype, or float32 with
     grad_dtype=torch.float32; one that is not needed is None and not
     computed.  piece_bytes bounds the piece of the logits' gradient that is
-    held at a time (0: 1 GiB).
+    held at a time (0: 1 GiB; float16 has room for two copies of it).
     """
     head = _ce_head(hidden, weight, target, (grad_loss, lse), ignore_index, logit_scale,
                     label_smoothing, z_loss, piece_bytes)

@@ -408,8 +408,12 @@ gemm_status_t gemm_ex_noalloc(const void *A, const void *B, void *C,
  * (piece_bytes).  hidden and weight are both FP16 or both BF16; products are
  * accumulated and all softmax statistics held in FP32.  In the backward
  * calls the gradient of the logits is rounded once to the 16-bit input type
- * (FP16: scaled by a power of two first, so that small probabilities stay
- * normal numbers) before the two products that take it.
+ * before the two products that take it.  It is scaled first so that the
+ * largest that a token can have is 1 (FP16: 2^14, which keeps probabilities
+ * down to 2^-28 normal numbers).  Where the tokens' weights in FP16 differ by
+ * more than a factor of 16, it is held twice, with a scale of its own for
+ * each token (for dhidden) and with one for all (for dweight), so that a
+ * token of little weight has a gradient as exact as the others'.
  *
  * Cross entropy (gemm_ce_*): with z = logits, lse = log sum_v exp z_v and
  * target t,
@@ -473,8 +477,9 @@ typedef struct {
     int32_t teacher_dtype;      /* teacher_logits: 0 = FP32, 1 = FP16, 2 = BF16 */
     int32_t top_k;              /* 1..GEMM_DISTILL_MAX_TOP_K */
     int64_t piece_bytes;        /* backward: largest piece of the logits' gradient held at a
-                                   time; 0 = GEMM_HEAD_PIECE_BYTES; at least 256 words' worth
-                                   are always held */
+                                   time (FP16: the workspace has room for two copies of it);
+                                   0 = GEMM_HEAD_PIECE_BYTES; at least 256 words' worth are
+                                   always held */
 } gemm_head_t;
 
 #define GEMM_DISTILL_MAX_TOP_K 256

@@ -134,3 +134,59 @@ def test_z_terms_of_any_size(g, z_loss, spread, shift, N, dtype):
     r = Gradients(H, W, t, gl, z_loss, F32)
     r.check("dhidden", dh)
     r.check("dweight", dw)
+
+
+def row_by_row(got, gl, unit):
+    """Rows of dhidden for weights gl that are powers of two, divided by them
+    (exact): each is bounded as the row of a call in which every token has
+    weight 1, whatever the others' weights are."""
+    x = got.detach().cpu().double() / gl.cpu().double()[:, None]
+    unit.check("dhidden", x)
+
+
+@pytest.mark.parametrize("N,V,D,piece", [(40, 5000, 64, 0), (300, 3001, 72, 0), (130, 2500, 101, 2 * 130 * 512),
+                                         (24, 40000, 40, 0)], ids=["few", "many", "pieces", "wide"])
+@pytest.mark.parametrize("kind", ["ce", "kd", "z"])
+def test_rows_of_little_weight(g, kind, N, V, D, piece):
+    # FP16, weights from 1 down to 2^-40, either sign, both gradients at once
+    # and each alone
+    H, W, t, _ = ref.inputs(N, V, D, F16, 74)
+    gl = (2.0 ** -torch.randint(0, 41, (N,), generator=torch.Generator().manual_seed(1)).double()).float()
+    gl[0], gl[1], gl[2] = 1.0, 2.0 ** -24, -2.0 ** -20
+    gl = gl.cuda()
+    one = torch.ones(N, device="cuda")
+    if kind == "kd":
+        at, a = ref.teacher(N, V, 9, F32, 74)
+        o = dict(temperature=2.0)
+        loss, lse = g.linear_distillation(H, W, at, a, **o)
+        back = lambda **k: g.linear_distillation_backward(gl, H, W, at, a, lse, grad_dtype=F32, piece_bytes=piece, **o, **k)
+        unit = ref.Reference(H, W, one, teacher_index=at, teacher_logits=a, grad_dtype=F32, **o)
+        r = ref.Reference(H, W, gl, teacher_index=at, teacher_logits=a, grad_dtype=F32, **o)
+    else:
+        o = dict(z_loss=1e-3) if kind == "z" else {}
+        t[6::7] = -100
+        loss, lse = g.linear_cross_entropy(H, W, t, **o)
+        back = lambda **k: g.linear_cross_entropy_backward(gl, H, W, t, lse, grad_dtype=F32, piece_bytes=piece, **o, **k)
+        unit = ref.Reference(H, W, one, target=t, grad_dtype=F32, **o)
+        r = ref.Reference(H, W, gl, target=t, grad_dtype=F32, **o)
+    dh, dw = back()
+    dh1, none = back(need_weight=False)
+    none, dw1 = back(need_hidden=False)
+    done(g)
+    row_by_row(dh, gl, unit)
+    r.check("dweight", dw)
+    assert torch.equal(dh, dh1)
+    r.check("dweight", dw1)
+
+
+def test_a_weight_that_is_not_finite_beside_small_ones(g):
+    H, W, t, _ = ref.inputs(50, 900, 64, F16, 75)
+    gl = torch.full((50,), 2.0 ** -30, device="cuda")
+    gl[0], gl[7], gl[8] = 1.0, math.inf, 0.0
+    loss, lse = g.linear_cross_entropy(H, W, t)
+    dh, dw = g.linear_cross_entropy_backward(gl, H, W, t, lse, grad_dtype=F32)
+    done(g)
+    assert not torch.isfinite(dh[7]).any() and not torch.isfinite(dw).any() and not dh[8].any()
+    keep = torch.tensor([i for i in range(50) if i not in (7, 8)])
+    unit = ref.Reference(H[keep], W, torch.ones(48, device="cuda"), target=t[keep], grad_dtype=F32)
+    row_by_row(dh[keep], gl[keep], unit)
