@@ -273,9 +273,12 @@ __global__ void __launch_bounds__(256) pack_rows_kernel(const uint16_t* in, int6
 
 // ---- the teacher's list ---------------------------------------------------------
 //
-// One warp to a token: softmax over the entries that are there, then the
-// entries in the order of their words (bitonic sort in shared memory), so
-// that a tile of the vocabulary finds its own entries as one run.
+// One warp to a token: softmax over the entries that are there (divided by the
+// temperature once the largest has been taken off: a finite logit may pass
+// FP32's range when it is divided first, and entries masked by their type's
+// lowest number are finite), then the entries in the order of their words
+// (bitonic sort in shared memory), so that a tile of the vocabulary finds its
+// own entries as one run.
 
 constexpr int kTeacherWarps = 8;
 constexpr int kTeacherMost = 256;
@@ -304,7 +307,7 @@ __global__ void __launch_bounds__(kTeacherWarps * 32) teacher_kernel(const Teach
             const float x = teacher_logit(a, n * a.ld_logits + j);
             if (w >= 0 && w < a.vocab && x != -INFINITY) {
                 word = static_cast<int32_t>(w);
-                t = x * a.inv_temperature;
+                t = x;
             }
         }
         key[j] = (static_cast<uint64_t>(static_cast<uint32_t>(word)) << 32) | static_cast<uint32_t>(j);
@@ -319,7 +322,7 @@ __global__ void __launch_bounds__(kTeacherWarps * 32) teacher_kernel(const Teach
     for (int j = lane; j < size; j += 32) {
         if (static_cast<int32_t>(key[j] >> 32) == kNoWord) continue;
         some = 1;
-        sum += expf(val[j] - top);
+        sum += expf((val[j] - top) / a.temperature);
     }
 #pragma unroll
     for (int o = 16; o; o >>= 1) sum += __shfl_xor_sync(~0u, sum, o);
@@ -346,7 +349,7 @@ __global__ void __launch_bounds__(kTeacherWarps * 32) teacher_kernel(const Teach
         const int32_t word = static_cast<int32_t>(x >> 32);
         a.words[n * a.top_k + j] = word;
         a.logq[n * a.top_k + j] =
-            word == kNoWord ? -INFINITY : val[static_cast<uint32_t>(x)] - top - log_sum;
+            word == kNoWord ? -INFINITY : (val[static_cast<uint32_t>(x)] - top) / a.temperature - log_sum;
     }
     if (lane == 0) a.active[n] = some ? 1 : 0;
 }

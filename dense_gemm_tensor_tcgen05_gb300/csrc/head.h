@@ -92,7 +92,7 @@ struct TeacherArgs {
     int dtype;   // 0 FP32, 1 FP16, 2 BF16
     int64_t tokens, vocab;
     int top_k;
-    float inv_temperature;
+    float temperature;
     int32_t* words;
     float* logq;
     uint8_t* active;

@@ -297,7 +297,7 @@ gemm_status_t begin(const gemm_head_t& h, int distill, const Layout& l, void* ws
         t.tokens = h.tokens;
         t.vocab = h.vocab;
         t.top_k = h.top_k;
-        t.inv_temperature = 1.0f / h.temperature;
+        t.temperature = h.temperature;
         t.words = r.words;
         t.logq = r.logq;
         t.active = r.active;

@@ -190,3 +190,24 @@ def test_a_weight_that_is_not_finite_beside_small_ones(g):
     keep = torch.tensor([i for i in range(50) if i not in (7, 8)])
     unit = ref.Reference(H[keep], W, torch.ones(48, device="cuda"), target=t[keep], grad_dtype=F32)
     row_by_row(dh[keep], gl[keep], unit)
+
+
+@pytest.mark.parametrize("dtype", [F32, BF16], ids=["f32", "bf16"])
+@pytest.mark.parametrize("T", [0.25, 0.5, 1.0, 4.0])
+def test_teacher_logits_at_the_ends_of_their_type(g, T, dtype):
+    # the lowest finite number counts for nothing beside others and for all
+    # where there are no others, at any temperature; so does the largest
+    H, W, _, gl = ref.inputs(40, 300, 64, BF16, 76)
+    at, a = ref.teacher(40, 300, 8, dtype, 76)
+    low, high = torch.finfo(dtype).min, torch.finfo(dtype).max
+    a[:, 4:] = low
+    a[7] = low
+    a[8, :2] = high
+    a[10] = high
+    at[7], at[10] = torch.arange(8, device="cuda"), torch.arange(8, device="cuda")
+    loss, lse = g.linear_distillation(H, W, at, a, temperature=T)
+    dh, dw = g.linear_distillation_backward(gl, H, W, at, a, lse, temperature=T)
+    done(g)
+    r = ref.Reference(H, W, gl, teacher_index=at, teacher_logits=a, temperature=T)
+    for name, x in (("loss", loss), ("lse", lse), ("dhidden", dh), ("dweight", dw)):
+        r.check(name, x)
