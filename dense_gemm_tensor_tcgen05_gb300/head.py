@@ -13,6 +13,12 @@ with grad_loss the gradient of what is optimised with respect to each token's
 loss (for the mean over the tokens: 1 / their number).  The formulas, the
 treatment of tokens without a target and the precision are those of
 include/gb300gemm.h.
+
+Every call returns at once; the work is on the current stream, or on the one
+given as ``stream``.  As with the C calls, what the stream waits for is the
+caller's: inputs made on another stream need ``stream.wait_stream(...)``
+first, and so does a stream that reads the results.  The inputs' memory is
+not given to anyone else before that stream is done with it.
 """
 from __future__ import annotations
 
@@ -160,10 +166,11 @@ def _distill_head(hidden, weight, index, logits, others, temperature, logit_scal
                     logits.data_ptr(), ld_logits, teacher_dtype, shape[1], piece_bytes)
 
 
-def _run(call, head, distill, backward, device, outputs, stream):
+def _run(call, head, distill, backward, device, inputs, outputs, stream):
     """Outputs and workspace from torch on the stream that the call runs on:
     `outputs` makes the tensors and gives what `call` takes between head and
-    workspace."""
+    workspace.  A caller may drop the inputs once the call has returned, so
+    torch is told when the stream is not the one that they were made on."""
     if stream is None:
         made, args = outputs()
         n = gemm_head_workspace(head, distill, backward)
@@ -175,12 +182,14 @@ def _run(call, head, distill, backward, device, outputs, stream):
             n = gemm_head_workspace(head, distill, backward)
             ws = torch.empty(n, dtype=torch.uint8, device=device)
         handle = stream.cuda_stream
+        for t in inputs:
+            t.record_stream(stream)
     call(head, *args, ws.data_ptr(), n, handle)
     return made
 
 
-def _forward(head, distill, hidden, stream):
-    device = hidden.device
+def _forward(head, distill, inputs, stream):
+    device = inputs[0].device
 
     def outputs():
         loss = torch.empty(head.tokens, dtype=torch.float32, device=device)
@@ -188,11 +197,11 @@ def _forward(head, distill, hidden, stream):
         return (loss, lse), (loss.data_ptr(), lse.data_ptr())
 
     return _run(gemm_distill_forward if distill else gemm_ce_forward, head, distill, 0, device,
-                outputs, stream)
+                inputs, outputs, stream)
 
 
-def _backward(head, distill, grad_loss, hidden, weight, lse, need_hidden, need_weight, grad_dtype,
-              stream):
+def _backward(head, distill, inputs, need_hidden, need_weight, grad_dtype, stream):
+    grad_loss, lse, hidden, weight = inputs[:4]
     dtype = hidden.dtype
     if grad_dtype is not None and grad_dtype != dtype:
         if grad_dtype != torch.float32:
@@ -212,7 +221,7 @@ def _backward(head, distill, grad_loss, hidden, weight, lse, need_hidden, need_w
                           dw.data_ptr() if need_weight else 0, dim or 1)
 
     return _run(gemm_distill_backward if distill else gemm_ce_backward, head, distill, 1, device,
-                outputs, stream)
+                inputs, outputs, stream)
 
 
 def linear_cross_entropy(hidden, weight, target, *, ignore_index=-100, logit_scale=1.0,
@@ -228,7 +237,7 @@ def linear_cross_entropy(hidden, weight, target, *, ignore_index=-100, logit_sca
     the current (or given) stream.
     """
     head = _ce_head(hidden, weight, target, (), ignore_index, logit_scale, label_smoothing, z_loss)
-    return _forward(head, 0, hidden, stream)
+    return _forward(head, 0, (hidden, weight, target), stream)
 
 
 def linear_cross_entropy_backward(grad_loss, hidden, weight, target, lse, *, ignore_index=-100,
@@ -246,8 +255,8 @@ def linear_cross_entropy_backward(grad_loss, hidden, weight, target, lse, *, ign
     """
     head = _ce_head(hidden, weight, target, (grad_loss, lse), ignore_index, logit_scale,
                     label_smoothing, z_loss, piece_bytes)
-    return _backward(head, 0, grad_loss, hidden, weight, lse, need_hidden, need_weight, grad_dtype,
-                     stream)
+    return _backward(head, 0, (grad_loss, lse, hidden, weight, target), need_hidden, need_weight,
+                     grad_dtype, stream)
 
 
 def linear_distillation(hidden, weight, teacher_index, teacher_logits, *, temperature=1.0,
@@ -263,7 +272,7 @@ def linear_distillation(hidden, weight, teacher_index, teacher_logits, *, temper
     without an entry has loss 0 and lse 0.
     """
     head = _distill_head(hidden, weight, teacher_index, teacher_logits, (), temperature, logit_scale)
-    return _forward(head, 1, hidden, stream)
+    return _forward(head, 1, (hidden, weight, teacher_index, teacher_logits), stream)
 
 
 def linear_distillation_backward(grad_loss, hidden, weight, teacher_index, teacher_logits, lse, *,
@@ -274,5 +283,5 @@ def linear_distillation_backward(grad_loss, hidden, weight, teacher_index, teach
     linear_cross_entropy_backward."""
     head = _distill_head(hidden, weight, teacher_index, teacher_logits, (grad_loss, lse),
                          temperature, logit_scale, piece_bytes)
-    return _backward(head, 1, grad_loss, hidden, weight, lse, need_hidden, need_weight, grad_dtype,
-                     stream)
+    return _backward(head, 1, (grad_loss, lse, hidden, weight, teacher_index, teacher_logits),
+                     need_hidden, need_weight, grad_dtype, stream)
