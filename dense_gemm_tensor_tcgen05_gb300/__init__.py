@@ -340,7 +340,7 @@ def matmul(A, B, out=None, stream=None, tf32=False, out_dtype=None, **opts):
     be row-major or column-major (a .t() view), on the GPU or the host.
     CUDA tensors run gemm_f16f32 / gemm_bf16f32 / sgemm_f32 (or gemm_ex when
     plan options are given) on the current (or given) stream and return at
-    once.  CPU tensors go through gemm_ex_host -- the library copies them in,
+    once; a given stream has to have waited for the one that made A and B.  CPU tensors go through gemm_ex_host -- the library copies them in,
     multiplies and copies C back, pipelined over row panels -- and the call
     returns the CPU result after synchronising the stream (pass page-locked
     tensors for overlapped copies).  ``opts`` are gemm_options_t fields
@@ -394,6 +394,9 @@ def matmul(A, B, out=None, stream=None, tf32=False, out_dtype=None, **opts):
     elif tuple(out.shape) != (M, N) or not out.is_cuda:
         raise ValueError("out must be a CUDA tensor of shape (M, N)")
     ldc = _row_major_ld(out, "C")
+    if stream is not None:   # the caller may drop its tensors before the stream has come to them
+        for t in (A, B, out):
+            t.record_stream(st)
     args = (A.data_ptr(), B.data_ptr(), out.data_ptr(), M, N, K, lda, ldb, ldc)
     sh = st.cuda_stream
     if opts:
