@@ -42,6 +42,11 @@ struct DeviceInfo {
 std::mutex g_dev_mu;
 std::map<int, DeviceInfo> g_dev;
 
+uint64_t current_ctx_id(int dev);
+
+// The current device, which the library can use, with a context current on
+// this host thread: its first CUDA call may be the encoding of a tensor map, a
+// driver call, which fails unless a context is current.
 gemm_status_t current_device(int* dev, DeviceInfo* info) {
     cudaError_t e = cudaGetDevice(dev);
     if (e != cudaSuccess) {
@@ -64,6 +69,7 @@ gemm_status_t current_device(int* dev, DeviceInfo* info) {
     }
     *info = d;
     if (d.major != 10 || d.minor != 3) return GEMM_ERR_UNSUPPORTED_DEVICE;
+    current_ctx_id(*dev);
     return GEMM_OK;
 }
 
@@ -806,9 +812,6 @@ gemm_status_t lib_device(int* dev, int* sms) {
     DeviceInfo info;
     const gemm_status_t st = current_device(dev, &info);
     *sms = info.sms;
-    // A host thread's first CUDA call may be the encoding of a tensor map, a
-    // driver call, which fails unless a context is current.
-    if (st == GEMM_OK) current_ctx_id(*dev);
     return st;
 }
 
@@ -1083,6 +1086,7 @@ gemm_status_t noalloc_device(int* dev, int* sms) {
         return GEMM_ERR_CUDA;
     }
     if (major != 10 || minor != 3) return GEMM_ERR_UNSUPPORTED_DEVICE;
+    current_ctx_id(*dev);   // as in current_device
     return GEMM_OK;
 }
 
