@@ -27,6 +27,9 @@ namespace {
 
 // Tiles past the last row or column still have 32-bit coordinates.
 constexpr int64_t kMostSize = (1ll << 31) - 1024;
+// Elements of a matrix: 2^12 times what the memory holds.  The workspace, at
+// most 64 FP32 parts and two copies of such matrices, stays far inside 64 bits.
+constexpr int64_t kMostElements = 1ll << 50;
 
 int64_t round_up(int64_t a, int64_t m) { return (a + m - 1) / m * m; }
 
@@ -55,6 +58,9 @@ gemm_status_t check_head(const gemm_head_t* h, int distill) {
     if (h->tokens < 0 || h->vocab < 0 || h->dim < 0 || h->tokens > kMostSize || h->vocab > kMostSize ||
         h->dim > kMostSize)
         return lib_invalid("tokens, vocab and dim must be in [0, 2^31 - 1024]");
+    if (h->tokens * h->vocab > kMostElements || h->tokens * h->dim > kMostElements ||
+        h->vocab * h->dim > kMostElements)
+        return lib_invalid("no two of tokens, vocab and dim may have a product above 2^50");
     if (h->ldh < h->dim || h->ldw < h->dim || far(h->tokens, h->ldh) || far(h->vocab, h->ldw))
         return lib_invalid("row stride of hidden or weight");
     if (!(h->logit_scale > 0.0f) || !std::isfinite(h->logit_scale)) return lib_invalid("logit_scale");

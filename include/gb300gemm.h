@@ -458,7 +458,8 @@ gemm_status_t gemm_ex_noalloc(const void *A, const void *B, void *C,
 typedef struct {
     int32_t dtype;              /* hidden and weight: 0 = FP16, 1 = BF16 */
     int32_t grad_dtype;         /* dhidden and dweight: 0 = as dtype, 1 = FP32 */
-    int64_t tokens, vocab, dim; /* each at most 2^31 - 1024; vocab >= 1 if tokens > 0 */
+    int64_t tokens, vocab, dim; /* each at most 2^31 - 1024, the product of any two at most
+                                   2^50; vocab >= 1 if tokens > 0 */
     const void *hidden;         /* tokens x dim, row stride ldh >= dim */
     int64_t ldh;
     const void *weight;         /* vocab x dim, row stride ldw >= dim */
