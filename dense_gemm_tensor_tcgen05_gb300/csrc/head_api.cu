@@ -91,6 +91,15 @@ gemm_status_t check_head(const gemm_head_t* h, int distill) {
     return GEMM_OK;
 }
 
+// The stride of a single row is never taken, whatever it is, but a tensor map
+// holds strides below 2^40 bytes only: one that suits the copies stands for it.
+gemm_head_t with_strides(const gemm_head_t& head) {
+    gemm_head_t h = head;
+    if (h.tokens <= 1) h.ldh = round_up(h.dim, 8);
+    if (h.vocab <= 1) h.ldw = round_up(h.dim, 8);
+    return h;
+}
+
 constexpr int kClusters = 76;   // CTA pairs of the 152 SMs; the workspace's size goes by it
 
 // Whether the two gradient products go in one launch, whose clusters share the
@@ -379,7 +388,7 @@ constexpr int kFewStatsChunk = 2, kStatsChunk = 3, kChunk = 8;
 gemm_status_t forward(const gemm_head_t* head, int distill, float* loss, float* lse, void* ws,
                       int64_t ws_bytes, gemm_stream_t stream_) {
     GB_TRY(check_head(head, distill));
-    const gemm_head_t& h = *head;
+    const gemm_head_t h = with_strides(*head);
     if (h.tokens == 0) return GEMM_OK;
     if (!loss || !lse || off(loss, 4) || off(lse, 4)) return lib_invalid("loss or lse is NULL or misaligned");
     const Layout l = layout_of(h, distill, 0);
@@ -432,11 +441,13 @@ gemm_status_t backward(const gemm_head_t* head, int distill, const float* lse, c
                        int64_t grad_stride, void* dhidden, int64_t lddh, void* dweight, int64_t lddw,
                        void* ws, int64_t ws_bytes, gemm_stream_t stream_) {
     GB_TRY(check_head(head, distill));
-    const gemm_head_t& h = *head;
+    const gemm_head_t h = with_strides(*head);
     const int ct = h.grad_dtype == 1 ? kCF32 : h.dtype == 1 ? kCBF16 : kCF16;
     const int64_t ge = c_elem_bytes(ct);
     if (dhidden && (lddh < h.dim || far(h.tokens, lddh) || off(dhidden, ge))) return lib_invalid("dhidden");
     if (dweight && (lddw < h.dim || far(h.vocab, lddw) || off(dweight, ge))) return lib_invalid("dweight");
+    if (h.vocab <= 1) lddw = h.dim;
+    if (h.tokens <= 1) lddh = h.dim;
     if (grad_stride < 0 || far(h.tokens, grad_stride)) return lib_invalid("grad_stride");
     const bool want_h = dhidden && h.tokens > 0 && h.dim > 0, want_w = dweight && h.vocab > 0 && h.dim > 0;
     if (!want_h && !want_w) return GEMM_OK;
@@ -630,7 +641,7 @@ extern "C" {
 gemm_status_t gemm_head_workspace(const gemm_head_t* head, int32_t distill, int32_t backward, int64_t* bytes) {
     if (!bytes || distill < 0 || distill > 1 || backward < 0 || backward > 1) return GEMM_ERR_INVALID_VALUE;
     GB_TRY(check_head(head, distill));
-    *bytes = head->tokens == 0 ? 0 : layout_of(*head, distill, backward).bytes;
+    *bytes = head->tokens == 0 ? 0 : layout_of(with_strides(*head), distill, backward).bytes;
     return GEMM_OK;
 }
 
