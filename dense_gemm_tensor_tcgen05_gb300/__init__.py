@@ -31,7 +31,7 @@ __all__ = [
     "gemm_alloc_count", "matmul", "gemm", "plan",
     "GemmOptions", "STATUS", "EXPORTED_SYMBOLS", "C_DTYPE",
     "HeadArgs", "gemm_head_workspace", "gemm_ce_forward", "gemm_ce_backward",
-    "gemm_distill_forward", "gemm_distill_backward", "linear_cross_entropy",
+    "gemm_distill_forward", "gemm_distill_backward", "gemm_ce_stall_selftest", "linear_cross_entropy",
     "linear_cross_entropy_backward", "linear_distillation", "linear_distillation_backward",
 ]
 
@@ -57,7 +57,7 @@ EXPORTED_SYMBOLS = (
     "gemm_ex_host", "gemm_watchdog_selftest", "gemm_tf32f32_bt", "gemm_e4m3f32_bt",
     "gemm_e5m2f32_bt", "gemm_ex_stall_selftest", "gemm_alloc_count",
     "gemm_head_workspace", "gemm_ce_forward", "gemm_ce_backward", "gemm_distill_forward",
-    "gemm_distill_backward",
+    "gemm_distill_backward", "gemm_ce_stall_selftest",
 )
 
 
@@ -136,6 +136,9 @@ def lib() -> ctypes.CDLL:
                 f = getattr(L, name)
                 f.argtypes = [head, vp, vp, vp, i64, vp]
                 f.restype = ctypes.c_int
+            L.gemm_ce_stall_selftest.argtypes = [head, vp, vp, vp, i64, ctypes.c_int32,
+                                                 ctypes.c_int32, ctypes.c_int32, vp]
+            L.gemm_ce_stall_selftest.restype = ctypes.c_int
             for name in ("gemm_ce_backward", "gemm_distill_backward"):
                 f = getattr(L, name)
                 f.argtypes = [head, vp, vp, i64, vp, i64, vp, i64, vp, i64, vp]
@@ -437,6 +440,6 @@ def plan(A, B, out=None, tf32=False, **opts) -> str:
 
 # The output layer's losses (cross entropy, distillation): their own file.
 from .head import (  # noqa: E402
-    gemm_ce_backward, gemm_ce_forward, gemm_distill_backward, gemm_distill_forward,
+    gemm_ce_backward, gemm_ce_forward, gemm_ce_stall_selftest, gemm_distill_backward, gemm_distill_forward,
     gemm_head_workspace, linear_cross_entropy, linear_cross_entropy_backward,
     linear_distillation, linear_distillation_backward)

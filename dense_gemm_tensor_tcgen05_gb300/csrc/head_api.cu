@@ -360,15 +360,19 @@ void logits_of(const gemm_head_t& h, const Layout& l, const GatherArgs& g, const
     p->w0 = w0;
 }
 
+// pairs resident at once; more than that would only wait their turn
+int clusters_at_once() {
+    const int clusters = lib_pair_clusters();
+    return clusters > 0 ? clusters : kClusters;
+}
+
 gemm_status_t run_gemm(const HeadGemm& p, const HeadGemm* and_then, cudaStream_t stream) {
     EncodeTiledFn encode = lib_encode_fn();
     if (!encode) {
         lib_invalid("cuTensorMapEncodeTiled entry point unavailable");
         return GEMM_ERR_CUDA;
     }
-    // pairs resident at once; more than that would only wait their turn
-    const int clusters = lib_pair_clusters();
-    return lib_launch_status(head_gemm_launch(p, and_then, clusters > 0 ? clusters : kClusters, encode, stream), "head_gemm");
+    return lib_launch_status(head_gemm_launch(p, and_then, clusters_at_once(), encode, stream), "head_gemm");
 }
 
 float scale_of(const gemm_head_t& h, int distill) {
@@ -385,8 +389,14 @@ constexpr float kLog2e = 1.4426950408889634f;
 // of 3 (16 x 131072 x 4096: 178 and 177 us; of 1: 191).
 constexpr int kFewStatsChunk = 2, kStatsChunk = 3, kChunk = 8;
 
+// A self-test of the tensor-core kernel's bounded waits (gemm_ce_stall_selftest).
+struct HeadStall {
+    uint64_t limit_ns;
+    int32_t cluster, fill;
+};
+
 gemm_status_t forward(const gemm_head_t* head, int distill, float* loss, float* lse, void* ws,
-                      int64_t ws_bytes, gemm_stream_t stream_) {
+                      int64_t ws_bytes, gemm_stream_t stream_, const HeadStall* stall = nullptr) {
     GB_TRY(check_head(head, distill));
     const gemm_head_t h = with_strides(*head);
     if (h.tokens == 0) return GEMM_OK;
@@ -400,6 +410,18 @@ gemm_status_t forward(const gemm_head_t* head, int distill, float* loss, float* 
     GB_TRY(lib_device(&dev, &sms));
     cudaStream_t stream = reinterpret_cast<cudaStream_t>(stream_);
 
+    HeadGemm p;
+    memset(&p, 0, sizeof(p));
+    if (stall) {
+        p.m = h.tokens;
+        p.n = h.vocab;
+        p.splits = 1;
+        if (stall->cluster < 0 || stall->cluster >= head_gemm_clusters(p, nullptr, clusters_at_once()) || stall->fill < 0)
+            return lib_invalid("stall self-test: stall_cluster or stall_fill");
+        p.wait_limit_ns = stall->limit_ns;
+        p.stall_cluster = stall->cluster;
+        p.stall_fill = stall->fill + 1;
+    }
     GatherArgs g;
     memset(&g, 0, sizeof(g));
     g.pad_rows = kHeadStepK;
@@ -407,8 +429,6 @@ gemm_status_t forward(const gemm_head_t* head, int distill, float* loss, float* 
     int64_t ldw;
     GB_TRY(begin(h, distill, l, ws, g, sms, stream, &weight, &ldw));
 
-    HeadGemm p;
-    memset(&p, 0, sizeof(p));
     p.mode = distill ? kHeadStatsKd : kHeadStatsCe;
     p.bf16 = h.dtype;
     p.rows = g.rows;
@@ -648,6 +668,14 @@ gemm_status_t gemm_head_workspace(const gemm_head_t* head, int32_t distill, int3
 gemm_status_t gemm_ce_forward(const gemm_head_t* head, float* loss, float* lse, void* workspace,
                               int64_t workspace_bytes, gemm_stream_t stream) {
     return forward(head, 0, loss, lse, workspace, workspace_bytes, stream);
+}
+
+gemm_status_t gemm_ce_stall_selftest(const gemm_head_t* head, float* loss, float* lse, void* workspace,
+                                     int64_t workspace_bytes, int32_t limit_ms, int32_t stall_cluster,
+                                     int32_t stall_fill, gemm_stream_t stream) {
+    if (limit_ms < 1 || limit_ms > 2000) return lib_invalid("limit_ms");
+    const HeadStall t{static_cast<uint64_t>(limit_ms) * 1000000ull, stall_cluster, stall_fill};
+    return forward(head, 0, loss, lse, workspace, workspace_bytes, stream, &t);
 }
 
 gemm_status_t gemm_distill_forward(const gemm_head_t* head, float* loss, float* lse, void* workspace,

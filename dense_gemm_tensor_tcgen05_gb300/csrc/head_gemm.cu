@@ -47,7 +47,8 @@
 //
 // Every wait gives up after two seconds, sets the device error word and
 // makes the pair leave; copies and products in flight are waited for
-// (bounded) and tensor memory is freed on every path.
+// (bounded) and tensor memory is freed on every path.  A self-test shortens
+// the limit and has one cluster withhold a stage.
 
 #include <algorithm>
 #include <cmath>
@@ -64,7 +65,7 @@ namespace {
 __device__ uint32_t g_head_error;   // bits as in the GEMM kernels' error word
 
 constexpr uint32_t kErrProducer = 1u, kErrMma = 2u, kErrEpilogue = 4u, kErrDrain = 8u;
-constexpr uint64_t kWaitNs = 2000000000ull, kDrainNs = 200000000ull, kPairDrainNs = 3 * kWaitNs;
+constexpr uint64_t kWaitNs = 2000000000ull, kDrainNs = 200000000ull, kPairDrainNs = 3 * kWaitNs;   // kWaitNs: default
 
 constexpr int kThreads = 384;
 constexpr int kFirstSumWarp = 4;
@@ -91,6 +92,10 @@ struct Args {
     // FEW: rows of P that the even CTA copies (the odd one none), and stages
     int32_t p_rows, stages;
     uint32_t idesc;
+    // how long a wait may take; the stage fill that the copying threads of
+    // one cluster withhold (self-test; -1 for both: none)
+    uint64_t wait_limit_ns;
+    int32_t stall_cluster, stall_fill;
     const int32_t* count;
     // output
     void* out;
@@ -126,6 +131,7 @@ struct Params {
 struct Wait {
     volatile uint32_t* abort_flag;   // this CTA's (the peer may raise it)
     uint32_t peer_abort;             // shared::cluster address of the peer's
+    const uint64_t* limit_ns;        // read by waits that have begun to wait
 };
 
 __device__ __forceinline__ void raise_abort(const Wait& w) {
@@ -141,7 +147,7 @@ __device__ __forceinline__ bool wait_phase(uint32_t bar, uint32_t parity, const 
     while (true) {
         if (done()) return true;
         if (*w.abort_flag) return false;
-        if (globaltimer_ns() - t0 > kWaitNs) {
+        if (globaltimer_ns() - t0 > *w.limit_ns) {
             atomicOr(&g_head_error, err);
             raise_abort(w);
             return false;
@@ -589,7 +595,8 @@ head_gemm_kernel(const __grid_constant__ Params first, const __grid_constant__ P
     tc_fence_after_sync();
     const uint32_t tmem = *tmem_slot;
     grid_dep_launch_dependents();
-    const Wait wait{abort_flag, mapa_shared(smem_u32(const_cast<uint32_t*>(abort_flag)), rank ^ 1u)};
+    const Wait wait{abort_flag, mapa_shared(smem_u32(const_cast<uint32_t*>(abort_flag)), rank ^ 1u),
+                    &first.a.wait_limit_ns};
     // every role reads global memory (the number of tokens, at least)
     grid_dep_wait();
     const int p_bytes = FEW ? 2 * first.a.p_rows * kRowBytes : kQBytes, stage_bytes = p_bytes + kQBytes;
@@ -612,7 +619,8 @@ head_gemm_kernel(const __grid_constant__ Params first, const __grid_constant__ P
                 int stage = 0;
                 uint32_t phase = 0, armed = 0, armed_parity = 0;
                 bool ok = true;
-                int items = 0;
+                int items = 0, fills = 0;
+                const int stall = static_cast<int>(cluster_id_x()) == first.a.stall_cluster ? first.a.stall_fill : -1;
                 while (ok && turns.next(two, u)) {
                     const Params& x = kTwo && two ? second : first;
                     const Args& a = x.a;
@@ -632,7 +640,9 @@ head_gemm_kernel(const __grid_constant__ Params first, const __grid_constant__ P
                         }
                         const uint32_t fb = mapa_shared(full_bar(stage), 0);
                         const uint32_t sp = base + stage * stage_bytes;
-                        if (p_side) {
+                        if (fills++ == stall) {
+                            // self-test: the pair's four copying threads leave this stage out
+                        } else if (p_side) {
                             if (leader) {   // all four threads' bytes complete on the even CTA's barrier
                                 mbar_arrive_expect_tx(full_bar(stage), static_cast<uint32_t>(
                                     FEW ? p_bytes + 2 * kQBytes : 2 * stage_bytes));
@@ -1048,6 +1058,9 @@ static bool params_of(const HeadGemm& g, int p_rows, int stages, EncodeTiledFn f
     a.p_rows = p_rows;
     a.stages = stages;
     a.idesc = idesc_f16_f32(g.bf16 ? 1u : 0u, !g.p.kmajor, !g.q.kmajor, kHeadTileM, kHeadTileN);
+    a.wait_limit_ns = g.wait_limit_ns ? g.wait_limit_ns : kWaitNs;
+    a.stall_cluster = g.stall_fill > 0 ? g.stall_cluster : -1;
+    a.stall_fill = g.stall_fill - 1;
     a.count = g.rows.count;
     a.out = g.out;
     a.ldo = g.ldo;
@@ -1084,6 +1097,10 @@ static bool params_of(const HeadGemm& g, int p_rows, int stages, EncodeTiledFn f
     return true;
 }
 
+int64_t head_gemm_clusters(const HeadGemm& g, const HeadGemm* and_then, int clusters) {
+    return std::min<int64_t>(units_of(g) + (and_then ? units_of(*and_then) : 0), clusters);
+}
+
 cudaError_t head_gemm_launch(const HeadGemm& g, const HeadGemm* and_then, int clusters, EncodeTiledFn fn,
                              cudaStream_t stream) {
     const int64_t units = units_of(g) + (and_then ? units_of(*and_then) : 0);
@@ -1101,7 +1118,7 @@ cudaError_t head_gemm_launch(const HeadGemm& g, const HeadGemm* and_then, int cl
     if (!params_of(g, p_rows, stages, fn, &first)) return cudaErrorInvalidValue;
     memset(&second, 0, sizeof(second));
     if (and_then && !params_of(*and_then, p_rows, stages, fn, &second)) return cudaErrorInvalidValue;
-    const int grid = 2 * static_cast<int>(std::min<int64_t>(units, clusters));
+    const int grid = 2 * static_cast<int>(head_gemm_clusters(g, and_then, clusters));
     const bool few = p_rows < 128;
     switch (g.mode) {
         case kHeadStatsCe: return launch<kHeadStatsCe>(grid, few, first, second, stream);

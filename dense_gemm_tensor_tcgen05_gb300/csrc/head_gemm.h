@@ -62,11 +62,18 @@ struct HeadGemm {
     int64_t ld_stats;
     float* z_at;
     const float *lse2, *gain, *boost;
+    // Self-test of the kernel's own bounded waits; 0 and 0 for ordinary calls.
+    uint64_t wait_limit_ns;  // 0: two seconds
+    int stall_cluster;       // cluster whose copying threads withhold one stage
+    int stall_fill;          // 1 + index of the stage fill they withhold; 0: none
 };
 
 // True if the output can leave through tensor stores: base and row stride on
 // 16-byte boundaries and rows that end on one (a store is clipped there).
 bool head_gemm_tensor_store(const void* out, int ct, int64_t inner, int64_t ld);
+
+// Clusters that a launch has, of `clusters` that fit at once.
+int64_t head_gemm_clusters(const HeadGemm& g, const HeadGemm* and_then, int clusters);
 
 // Launches one product, or two that do not depend on each other (products
 // only; the one with the longer K first) as one kernel.

@@ -50,6 +50,13 @@ def gemm_ce_forward(head: HeadArgs, loss: int, lse: int, workspace: int, workspa
     _check(lib().gemm_ce_forward(head, loss, lse, workspace, workspace_bytes, stream or None))
 
 
+def gemm_ce_stall_selftest(head: HeadArgs, loss: int, lse: int, workspace: int,
+                           workspace_bytes: int, limit_ms: int, stall_cluster: int, stall_fill: int,
+                           stream: int = 0) -> None:
+    _check(lib().gemm_ce_stall_selftest(head, loss, lse, workspace, workspace_bytes, limit_ms,
+                                        stall_cluster, stall_fill, stream or None))
+
+
 def gemm_ce_backward(head: HeadArgs, lse: int, grad_loss: int, grad_stride: int, dhidden: int,
                      lddh: int, dweight: int, lddw: int, workspace: int, workspace_bytes: int,
                      stream: int = 0) -> None:

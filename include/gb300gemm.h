@@ -503,6 +503,18 @@ gemm_status_t gemm_ce_backward(const gemm_head_t *head, const float *lse, const 
                                int64_t lddw, void *workspace, int64_t workspace_bytes,
                                gemm_stream_t stream);
 
+/* gemm_ce_stall_selftest -- checks the failure path of the losses' kernel, as
+ * gemm_ex_stall_selftest does for the GEMM's: gemm_ce_forward in which every
+ * pipeline wait gives up after limit_ms (1..2000) milliseconds and cluster
+ * `stall_cluster` (below min(256 x 256 tiles of the logits, CTA pairs on the
+ * device)) withholds the copies of its pipeline stage number `stall_fill`.
+ * gemm_device_error then returns GEMM_ERR_DEVICE_TIMEOUT once; loss and lse
+ * are unspecified, later calls are right. */
+gemm_status_t gemm_ce_stall_selftest(const gemm_head_t *head, float *loss, float *lse,
+                                     void *workspace, int64_t workspace_bytes, int32_t limit_ms,
+                                     int32_t stall_cluster, int32_t stall_fill,
+                                     gemm_stream_t stream);
+
 gemm_status_t gemm_distill_forward(const gemm_head_t *head, float *loss, float *lse,
                                    void *workspace, int64_t workspace_bytes, gemm_stream_t stream);
 
