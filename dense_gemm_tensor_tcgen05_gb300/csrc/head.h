@@ -50,7 +50,7 @@ __device__ __forceinline__ int32_t head_target(const int64_t* target, int64_t st
 // (backward), it also lays out by place what the logits' gradient takes:
 // lse2 = lse log2 e, gain = grad_loss / top * unit and boost = 1 + 2 z_loss
 // lse, and writes the factor that undoes the gain's scaling, factor = top *
-// undo, also for each row (undo_row).  top is the largest of size = |grad_loss|
+// undo.  top is the largest of size = |grad_loss|
 // (1 + |2 z_loss lse|), which bounds a token's gradient of the logits, so that
 // none passes unit in size.  It is the largest of the finite ones: an infinite
 // or NaN grad_loss stays with its token's row, and with the sums that the row
@@ -58,9 +58,9 @@ __device__ __forceinline__ int32_t head_target(const int64_t* target, int64_t st
 // by_row (a type with few exponents, and dhidden is wanted): where sizes
 // differ by more than kHeadSpread, a row of dhidden would be summed from
 // numbers that fall below the type's normal ones.  *spread is then 1, every
-// row has a gain of its own, unit / (1 + |2 z_loss lse|), undone by
-// undo_row, and ratio turns it into the gain relative to top, which dweight
-// needs, as its sums run over rows.
+// row has a gain of its own, unit / (1 + |2 z_loss lse|), and ratio turns it
+// into the gain relative to top, which dweight needs, as its sums run over
+// rows.  undo_row undoes a row's gain, whichever it is.
 // With zero_rows, the rows there of tokens without a target are zeroed
 // (element type zero_ct).
 struct GatherArgs {

@@ -537,6 +537,7 @@ gemm_status_t backward(const gemm_head_t* head, int distill, const float* lse, c
     d.out_outer = h.tokens;
     // without dweight the only copy is the one by rows
     if (g.by_row && want_w) {
+        d.mode = distill ? kHeadGradKdRows : kHeadGradCeRows;
         d.spread = g.spread;
         d.by_row = at<uint16_t>(ws, l.by_row);
         d.ratio = g.ratio;
@@ -562,7 +563,8 @@ gemm_status_t backward(const gemm_head_t* head, int distill, const float* lse, c
         ph.ldo = lddh;
         ph.out_outer = h.tokens;
         ph.out_perm = g.rows.perm;
-        ph.row_factor = g.undo_row;
+        ph.factor = g.factor;
+        ph.row_factor = g.by_row ? g.undo_row : nullptr;
     } else {
         ph.out = at<float>(ws, l.dh);
         ph.ct = kCF32;
@@ -648,7 +650,7 @@ gemm_status_t backward(const gemm_head_t* head, int distill, const float* lse, c
         s.part_stride = l.np * l.dp;
         s.rank = g.rows.rank;
         s.count = g.rows.count;
-        s.row_factor = g.undo_row;
+        s.row_factor = g.by_row ? g.undo_row : nullptr;
         GB_TRY(lib_launch_status(sum_rows_launch(s, sms, stream), "sum_rows"));
     }
     return GEMM_OK;

@@ -48,7 +48,7 @@
 // Every wait gives up after two seconds, sets the device error word and
 // makes the pair leave; copies and products in flight are waited for
 // (bounded) and tensor memory is freed on every path.  A self-test shortens
-// the limit and has one cluster withhold a stage.
+// the limit and has one cluster's copies stop.
 
 #include <algorithm>
 #include <cmath>
@@ -92,8 +92,8 @@ struct Args {
     // FEW: rows of P that the even CTA copies (the odd one none), and stages
     int32_t p_rows, stages;
     uint32_t idesc;
-    // how long a wait may take; the stage fill that the copying threads of
-    // one cluster withhold (self-test; -1 for both: none)
+    // how long a wait may take; the stage from which on the copying threads
+    // of one cluster withhold their copies (self-test; cluster -1: none)
     uint64_t wait_limit_ns;
     int32_t stall_cluster, stall_fill;
     const int32_t* count;
@@ -131,7 +131,7 @@ struct Params {
 struct Wait {
     volatile uint32_t* abort_flag;   // this CTA's (the peer may raise it)
     uint32_t peer_abort;             // shared::cluster address of the peer's
-    const uint64_t* limit_ns;        // read by waits that have begun to wait
+    volatile uint64_t* limit_ns;     // this CTA's copy of the launch's limit
 };
 
 __device__ __forceinline__ void raise_abort(const Wait& w) {
@@ -143,11 +143,11 @@ template <bool CLUSTER>
 __device__ __forceinline__ bool wait_phase(uint32_t bar, uint32_t parity, const Wait& w, uint32_t err) {
     auto done = [&]() { return CLUSTER ? mbar_try_wait_cluster(bar, parity) : mbar_try_wait(bar, parity); };
     if (done()) return true;
-    const uint64_t t0 = globaltimer_ns();
+    const uint64_t last = globaltimer_ns() + *w.limit_ns;
     while (true) {
         if (done()) return true;
         if (*w.abort_flag) return false;
-        if (globaltimer_ns() - t0 > *w.limit_ns) {
+        if (globaltimer_ns() > last) {
             atomicOr(&g_head_error, err);
             raise_abort(w);
             return false;
@@ -566,6 +566,7 @@ head_gemm_kernel(const __grid_constant__ Params first, const __grid_constant__ P
     const uint32_t drain_bar = bar0 + 8u * (2 * kMaxStages + 4);
     uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(bars + kBars);
     volatile uint32_t* abort_flag = tmem_slot + 1;
+    volatile uint64_t* limit_ns = reinterpret_cast<volatile uint64_t*>(tmem_slot + 2);
 
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
     const uint32_t rank = cluster_ctarank();
@@ -582,6 +583,7 @@ head_gemm_kernel(const __grid_constant__ Params first, const __grid_constant__ P
         }
         mbar_init(drain_bar, 1);
         *abort_flag = 0;
+        *limit_ns = first.a.wait_limit_ns;
         fence_barrier_init();
         tma_prefetch_map(&first.p);
         tma_prefetch_map(&first.q);
@@ -596,7 +598,7 @@ head_gemm_kernel(const __grid_constant__ Params first, const __grid_constant__ P
     const uint32_t tmem = *tmem_slot;
     grid_dep_launch_dependents();
     const Wait wait{abort_flag, mapa_shared(smem_u32(const_cast<uint32_t*>(abort_flag)), rank ^ 1u),
-                    &first.a.wait_limit_ns};
+                    limit_ns};
     // every role reads global memory (the number of tokens, at least)
     grid_dep_wait();
     const int p_bytes = FEW ? 2 * first.a.p_rows * kRowBytes : kQBytes, stage_bytes = p_bytes + kQBytes;
@@ -619,8 +621,14 @@ head_gemm_kernel(const __grid_constant__ Params first, const __grid_constant__ P
                 int stage = 0;
                 uint32_t phase = 0, armed = 0, armed_parity = 0;
                 bool ok = true;
-                int items = 0, fills = 0;
-                const int stall = static_cast<int>(cluster_id_x()) == first.a.stall_cluster ? first.a.stall_fill : -1;
+                int items = 0;
+                // self-test: the tile in which the pair's four copying threads
+                // stop, and after how many of its stages
+                int stall_item = -1, stall_step = 0;
+                if (static_cast<int>(cluster_id_x()) == first.a.stall_cluster && w1.steps > 0) {
+                    stall_item = first.a.stall_fill / w1.steps;
+                    stall_step = first.a.stall_fill % w1.steps;
+                }
                 while (ok && turns.next(two, u)) {
                     const Params& x = kTwo && two ? second : first;
                     const Args& a = x.a;
@@ -628,11 +636,13 @@ head_gemm_kernel(const __grid_constant__ Params first, const __grid_constant__ P
                     const int r0 = (p_side ? it.pb * kHeadTileM : it.qb * kHeadTileN) + static_cast<int>(rank) * 128;
                     // every other unit walks K backwards: it starts on the operand
                     // slices that the wave before it read last (still in L2)
-                    const bool down = (items++ & 1) != 0;
+                    const bool down = (items & 1) != 0;
+                    const int k_end = items == stall_item ? it.k0 + stall_step : it.k1;
+                    ok = items++ != stall_item;
                     const bool alt = kTwo && two ? alt2 : alt1;
                     const CUtensorMap* map = !p_side ? &x.q : alt ? &x.by_row : &x.p;
                     const bool kmajor = p_side ? a.p_kmajor : a.q_kmajor;
-                    for (int s = it.k0; s < it.k1; ++s) {
+                    for (int s = it.k0; s < k_end; ++s) {
                         const int ks = down ? it.k1 - 1 - (s - it.k0) : s;
                         if (!wait_phase<false>(empty_bar(stage), phase ^ 1u, wait, kErrProducer)) {
                             ok = false;
@@ -640,9 +650,7 @@ head_gemm_kernel(const __grid_constant__ Params first, const __grid_constant__ P
                         }
                         const uint32_t fb = mapa_shared(full_bar(stage), 0);
                         const uint32_t sp = base + stage * stage_bytes;
-                        if (fills++ == stall) {
-                            // self-test: the pair's four copying threads leave this stage out
-                        } else if (p_side) {
+                        if (p_side) {
                             if (leader) {   // all four threads' bytes complete on the even CTA's barrier
                                 mbar_arrive_expect_tx(full_bar(stage), static_cast<uint32_t>(
                                     FEW ? p_bytes + 2 * kQBytes : 2 * stage_bytes));
@@ -736,9 +744,10 @@ head_gemm_kernel(const __grid_constant__ Params first, const __grid_constant__ P
         Turns turns(w1, w1.steps / first.a.splits, w2, kTwo && second.a.splits ? w2.steps / second.a.splits : 0);
         bool two;
         int u;
-        constexpr bool kKd = MODE == kHeadStatsKd || MODE == kHeadGradKd;
+        constexpr bool kRows = MODE == kHeadGradCeRows || MODE == kHeadGradKdRows;
+        constexpr bool kKd = MODE == kHeadStatsKd || MODE == kHeadGradKd || MODE == kHeadGradKdRows;
         constexpr bool kStats = MODE == kHeadStatsCe || MODE == kHeadStatsKd;
-        constexpr bool kGrad = MODE == kHeadGradCe || MODE == kHeadGradKd;
+        constexpr bool kGrad = MODE == kHeadGradCe || MODE == kHeadGradKd || kRows;
         const int quarter = warp & 3;                   // tensor-memory lanes 32 * quarter ..
         const int half = (warp - kFirstSumWarp) >> 2;   // columns 128 * half ..
         const uint32_t box = base + kRingBytes + static_cast<uint32_t>(warp - kFirstSumWarp) * 4096u;
@@ -748,7 +757,7 @@ head_gemm_kernel(const __grid_constant__ Params first, const __grid_constant__ P
         const uint32_t lanes = (static_cast<uint32_t>(quarter * 32) << 16) + static_cast<uint32_t>(half * kCols);
         const float factor1 = MODE == kHeadProduct && first.a.factor ? *first.a.factor : 1.0f;
         const float factor2 = kTwo && second.a.factor ? *second.a.factor : 1.0f;
-        const bool spread = kGrad && first.a.spread && *first.a.spread;
+        const bool spread = kRows && *first.a.spread;
         int acc = 0;
         uint32_t acc_phase = 0;
         bool ok = true;
@@ -771,7 +780,7 @@ head_gemm_kernel(const __grid_constant__ Params first, const __grid_constant__ P
                 lse2 = a.lse2[row];
                 gain = a.gain[row];
                 boost = a.boost[row];
-                if (spread) ratio = a.ratio[row];
+                if (kRows && spread) ratio = a.ratio[row];
             }
             float v[kCols];
             if (it.k0 == it.k1) {   // the empty sum
@@ -916,11 +925,13 @@ head_gemm_kernel(const __grid_constant__ Params first, const __grid_constant__ P
                 }
                 __syncwarp();
                 const Out to(a);
-                if (spread) {   // the copy with a scale for each row, then the common one
-                    store_boxes(to, &x.by_row, box, box, v, lane, row0, row0, col0);
+                // where weights differ, the copy with a scale for each row first
+#pragma unroll 1
+                for (bool by_row = kRows && spread;; by_row = false) {
+                    store_boxes(to, by_row ? &x.by_row : &x.o, box, box, v, lane, row0, row0, col0);
+                    if (!by_row) break;
                     scale_all(v, ratio);
                 }
-                store_boxes(to, &x.o, box, box, v, lane, row0, row0, col0);
             } else {
                 if (!some) continue;
                 const Out to(a);
@@ -1042,7 +1053,7 @@ static bool params_of(const HeadGemm& g, int p_rows, int stages, EncodeTiledFn f
                 CU_TENSOR_MAP_L2_PROMOTION_L2_256B))
         return false;
     // slices, sums onto the output and the logits' gradient leave through tensor stores only
-    if (!a.tensor_store && (g.splits > 1 || g.add || g.mode == kHeadGradCe || g.mode == kHeadGradKd)) return false;
+    if (!a.tensor_store && (g.splits > 1 || g.add || (g.out && g.mode != kHeadProduct))) return false;
     a.m = static_cast<int32_t>(g.m);
     a.n = static_cast<int32_t>(g.n);
     a.k = static_cast<int32_t>(g.k);
@@ -1124,6 +1135,8 @@ cudaError_t head_gemm_launch(const HeadGemm& g, const HeadGemm* and_then, int cl
         case kHeadStatsCe: return launch<kHeadStatsCe>(grid, few, first, second, stream);
         case kHeadStatsKd: return launch<kHeadStatsKd>(grid, few, first, second, stream);
         case kHeadGradCe: return launch<kHeadGradCe>(grid, few, first, second, stream);
+        case kHeadGradCeRows: return launch<kHeadGradCeRows>(grid, few, first, second, stream);
+        case kHeadGradKdRows: return launch<kHeadGradKdRows>(grid, few, first, second, stream);
         case kHeadGradKd: return launch<kHeadGradKd>(grid, few, first, second, stream);
         case kHeadProduct: return launch<kHeadProduct>(grid, few, first, second, stream);
     }

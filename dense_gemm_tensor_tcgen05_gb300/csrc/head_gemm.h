@@ -19,7 +19,11 @@ enum HeadMode {
     kHeadStatsKd = 1,    // the same, and the logits at the teacher's words
     kHeadGradCe = 2,     // the logits' gradient, 16 bits
     kHeadGradKd = 3,
-    kHeadProduct = 4     // the products themselves
+    kHeadProduct = 4,    // the products themselves
+    // the logits' gradient with its copy by rows: forms of their own, since
+    // holding a tile for a second store costs 2 us of 170 (4096 x 32001 x 2048)
+    kHeadGradCeRows = 5,
+    kHeadGradKdRows = 6
 };
 
 // A 16-bit matrix as it is stored: `outer` rows of `inner` elements, `ld`
@@ -64,8 +68,8 @@ struct HeadGemm {
     const float *lse2, *gain, *boost;
     // Self-test of the kernel's own bounded waits; 0 and 0 for ordinary calls.
     uint64_t wait_limit_ns;  // 0: two seconds
-    int stall_cluster;       // cluster whose copying threads withhold one stage
-    int stall_fill;          // 1 + index of the stage fill they withhold; 0: none
+    int stall_cluster;       // cluster whose copying threads stop
+    int stall_fill;          // 1 + number of stages they fill before; 0: they do not stop
 };
 
 // True if the output can leave through tensor stores: base and row stride on

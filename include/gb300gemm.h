@@ -507,7 +507,7 @@ gemm_status_t gemm_ce_backward(const gemm_head_t *head, const float *lse, const 
  * gemm_ex_stall_selftest does for the GEMM's: gemm_ce_forward in which every
  * pipeline wait gives up after limit_ms (1..2000) milliseconds and cluster
  * `stall_cluster` (below min(256 x 256 tiles of the logits, CTA pairs on the
- * device)) withholds the copies of its pipeline stage number `stall_fill`.
+ * device)) withholds its copies after `stall_fill` pipeline stages.
  * gemm_device_error then returns GEMM_ERR_DEVICE_TIMEOUT once; loss and lse
  * are unspecified, later calls are right. */
 gemm_status_t gemm_ce_stall_selftest(const gemm_head_t *head, float *loss, float *lse,

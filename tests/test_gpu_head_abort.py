@@ -1,7 +1,7 @@
 """The losses' tensor-core kernel when a pipeline wait runs out.
 
 gemm_ce_stall_selftest runs an ordinary cross-entropy call with every wait
-limited to some milliseconds and one cluster's copies of one stage withheld.
+limited to some milliseconds and one cluster's copies withheld from a stage on.
 The kernel gives up and returns, gemm_device_error says so once, and the next
 call is right, bit for bit.  Nothing faults or hangs."""
 from __future__ import annotations
@@ -57,7 +57,7 @@ SIZES = [(20, 2000, 1024), (200, 2000, 1024), (600, 2000, 1024), (600, 40000, 51
 
 @pytest.mark.parametrize("size", SIZES, ids=lambda s: "x".join(map(str, s)))
 @pytest.mark.parametrize("fill", [0, 2, 5])
-def test_a_withheld_stage_times_out_and_the_next_call_is_right(g, size, fill):
+def test_withheld_copies_time_out_and_the_next_call_is_right(g, size, fill):
     c = Call(g, *size)
     want = c.plain()
     began = time.perf_counter()
