@@ -25,6 +25,8 @@ import argparse
 def train(tokens=2048, vocab=32768, dim=1024, top_k=32, temperature=2.0, steps=20, rate=0.1, seed=1,
           say=print):
     """The mean losses of the first and of the last step: ((ce, kd), (ce, kd))."""
+    if steps < 1:
+        raise ValueError("steps must be at least 1")
     import torch
 
     import dense_gemm_tensor_tcgen05_gb300 as g
@@ -46,7 +48,7 @@ def train(tokens=2048, vocab=32768, dim=1024, top_k=32, temperature=2.0, steps=2
         prompt = torch.rand(tokens, **dev) < 0.25
         target[prompt] = -100
         words[prompt] = -1
-        each = (1.0 / (~prompt).sum()).float()
+        each = (1.0 / (~prompt).sum().clamp(min=1)).float()   # a batch of prompts only takes no step
         weight = master.bfloat16()
         begin.record()
         ce, lse = g.linear_cross_entropy(hidden, weight, target)
@@ -57,7 +59,7 @@ def train(tokens=2048, vocab=32768, dim=1024, top_k=32, temperature=2.0, steps=2
                                                need_hidden=False, grad_dtype=torch.float32)
         end.record()
         down = d1 + d2
-        master -= down * (rate * master.norm() / down.norm())
+        master -= down * (rate * master.norm() / down.norm().clamp(min=1e-30))
         seen.append((float(ce.sum() * each), float(kd.sum() * each)))
         g.gemm_device_error(torch.cuda.current_stream().cuda_stream)
         if step:
