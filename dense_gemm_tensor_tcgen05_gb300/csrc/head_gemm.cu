@@ -26,10 +26,11 @@
 // warps' stores to global memory and cost a quarter of the time.
 //
 // What bounds it.  Long products run at the tensor cores' power-limited rate:
-// 8192 x 131072 x 4096 takes 5.04 ms with the statistics (1744 TFLOP/s; the
-// same product alone, with a 16-bit result written, 1700 to 1780 by this
-// library's GEMM).  With few tokens the weight's read is the bound: 16 x
-// 65536 x 4096 takes 97 us, 5.5 TB/s.  Below a thousand channels the forming
+// 8192 x 131072 x 4096 takes 4.7 to 5.0 ms with the statistics, by the card
+// (1750 to 1870 TFLOP/s; the same product alone, with a 16-bit result written,
+// 1700 to 1780 by this library's GEMM where the statistics ran at 1744).  With
+// few tokens the weight's read is the bound: 16 x 65536 x 4096 takes 94 us,
+// 5.7 TB/s.  Below a thousand channels the forming
 // of a tile's results (128 exponentials a thread) takes as long as its
 // products.
 //

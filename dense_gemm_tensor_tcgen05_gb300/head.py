@@ -10,7 +10,9 @@ training step is
     dhidden, dweight = linear_cross_entropy_backward(grad_loss, hidden, weight, target, lse)
 
 with grad_loss the gradient of what is optimised with respect to each token's
-loss (for the mean over the tokens: 1 / their number).  The formulas, the
+loss (for the mean over the tokens: 1 / their number).  autograd does not see
+these calls: their results have no graph, also where hidden or weight requires
+a gradient, so the backward call has to be made.  The formulas, the
 treatment of tokens without a target and the precision are those of
 include/gb300gemm.h.
 
@@ -241,7 +243,7 @@ def linear_cross_entropy(hidden, weight, target, *, ignore_index=-100, logit_sca
     row-major with any row stride.  target: int64, one word for each token;
     a token with target == ignore_index has loss 0 and lse 0.  See
     include/gb300gemm.h for label_smoothing and z_loss.  Returns at once, on
-    the current (or given) stream.
+    the current (or given) stream, without a graph for autograd.
     """
     head = _ce_head(hidden, weight, target, (), ignore_index, logit_scale, label_smoothing, z_loss)
     return _forward(head, 0, (hidden, weight, target), stream)
@@ -256,7 +258,8 @@ def linear_cross_entropy_backward(grad_loss, hidden, weight, target, lse, *, ign
     grad_loss: float32, one number for each token (any stride) or a single
     one for all.  lse: the forward call's; the other arguments are those of
     the forward call.  Gradients have hidden's dtype, or float32 with
-    grad_dtype=torch.float32; one that is not needed is None and not
+    grad_dtype=torch.float32 (not rounded again, but with the errors of the
+    logits' gradient, which is held in hidden's dtype); one that is not needed is None and not
     computed.  piece_bytes bounds the piece of the logits' gradient that is
     held at a time (0: 1 GiB; float16 has room for two copies of it).
     """

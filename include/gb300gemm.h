@@ -402,12 +402,12 @@ gemm_status_t gemm_ex_noalloc(const void *A, const void *B, void *C,
  *
  * The four calls below compute a loss of these logits for each token, and
  * its gradient with respect to hidden and weight, without a tokens x vocab
- * matrix: the forward calls keep two numbers for each token and 256 words,
- * the backward calls form the logits' gradient again from hidden, weight and
- * the saved log-sum-exp, for one piece of the vocabulary at a time
- * (piece_bytes).  hidden and weight are both FP16 or both BF16; products are
- * accumulated and all softmax statistics held in FP32.  In the backward
- * calls the gradient of the logits is rounded once to the 16-bit input type
+ * matrix: the forward calls keep two numbers for each token and 128 words
+ * (three with label smoothing), the backward calls form the logits' gradient
+ * again from hidden, weight and the saved log-sum-exp, for one piece of the
+ * vocabulary at a time (piece_bytes).  hidden and weight are both FP16 or
+ * both BF16; products are accumulated and all softmax statistics held in
+ * FP32.  In the backward calls the gradient of the logits is rounded once to the 16-bit input type
  * before the two products that take it.  It is scaled first so that the
  * largest that a token can have is 1 (FP16: 2^14, which keeps probabilities
  * down to 2^-28 normal numbers).  Where the tokens' weights in FP16 differ by
@@ -438,12 +438,17 @@ gemm_status_t gemm_ex_noalloc(const void *A, const void *B, void *C,
  * logits / temperature.
  *
  * Tokens without a target cost nothing in the products: the calls gather the
- * others first.  Every sum is taken in a fixed order, so results do not
+ * others first (a forward call of up to 256 tokens, one row of tiles anyway,
+ * reads hidden in place if its base is on a 16-byte boundary and ldh a
+ * multiple of 8).  Every sum is taken in a fixed order, so results do not
  * change from run to run.
  *
  * grad_loss holds the gradient of whatever follows with respect to each
- * token's loss; grad_stride 0 reads one number for all tokens.  dhidden or
- * dweight may be NULL when that gradient is not wanted.
+ * token's loss; grad_stride 0 reads one number for all tokens.  One that is
+ * infinite or NaN reaches its token's row of dhidden and the whole of dweight,
+ * which sums over tokens, and no other row of dhidden.  dhidden or dweight may be NULL when that gradient is not wanted.
+ * FP32 gradients (grad_dtype 1) are not rounded again, but carry the rounding
+ * of the logits' gradient: relative errors are those of the 16-bit type.
  *
  * Any row stride and 2-byte alignment of hidden and weight is accepted; a
  * weight whose base is not on a 16-byte boundary or whose ldw is not a
