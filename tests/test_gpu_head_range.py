@@ -211,3 +211,23 @@ def test_teacher_logits_at_the_ends_of_their_type(g, T, dtype):
     r = ref.Reference(H, W, gl, teacher_index=at, teacher_logits=a, temperature=T)
     for name, x in (("loss", loss), ("lse", lse), ("dhidden", dh), ("dweight", dw)):
         r.check(name, x)
+
+
+def test_a_graph_takes_weights_of_either_kind(g):
+    # captured with equal weights, replayed with ones that differ much: the
+    # device decides at every replay
+    N, V, D = 90, 1500, 64
+    H, W, t, _ = ref.inputs(N, V, D, F16, 77)
+    gl = torch.ones(N, device="cuda")
+    loss, lse = g.linear_cross_entropy(H, W, t)
+    g.linear_cross_entropy_backward(gl, H, W, t, lse, grad_dtype=F32)      # loads the kernels
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph):
+        dh, dw = g.linear_cross_entropy_backward(gl, H, W, t, lse, grad_dtype=F32)
+    unit = ref.Reference(H, W, torch.ones(N, device="cuda"), target=t, grad_dtype=F32)
+    for low in (0, 30, 0):
+        gl.copy_((2.0 ** -(torch.arange(N) % (low + 1)).double()).float())
+        graph.replay()
+        done(g)
+        row_by_row(dh, gl, unit)
+        ref.Reference(H, W, gl, target=t, grad_dtype=F32).check("dweight", dw)
